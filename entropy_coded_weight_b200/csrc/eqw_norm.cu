@@ -11,6 +11,13 @@
 // codes: they come from one maximum and two fp32 roundings, so they do not
 // depend on the order in which the squares are summed.
 //
+// Squares leave the fp32 range long before the values do.  A row whose sum of
+// squares reaches 2^126 (or is no number) is normalised from h 2^-80, an exact
+// scaling that cancels out of the output and of the scale:
+//   rstd = 2^-80 / sqrt(mean (h 2^-80)^2 + eps 2^-160)
+// It rounds only what is below 2^-46, 100 binary orders under the row's own
+// root mean square.  Rows of ordinary size pay one comparison per thread and one per row.
+//
 // Bound by memory: x and res are read once, res_out, out and the scale written
 // once; a token's h stays in registers between the sum and the output.  One
 // row (token) is shared by T threads that hold E values each, as vectors of 8
@@ -33,6 +40,8 @@ namespace {
 constexpr uint32_t kMaxThreads = 1024;
 constexpr uint32_t kMaxPerThread = 32;
 constexpr uint32_t kMaxNormCols = kMaxThreads * kMaxPerThread;
+constexpr float kLargeSum = 0x1p126f;  // of squares, from which a row is scaled
+constexpr float kScaleDown = 0x1p-80f;  // 32768 squares of 2^128 2^-80 stay in range
 
 struct NormParams {
     const void *x;
@@ -106,6 +115,15 @@ __device__ __forceinline__ void store1(void *p, uint64_t at, float v) {
         static_cast<float *>(p)[at] = v;
     else
         static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v);
+}
+
+// The T threads of the block's row `sub`; a block whose rows have several warps each holds at most two.
+__device__ __forceinline__ void row_sync(uint32_t sub, uint32_t T) {
+    __syncwarp();
+    if (sub == 0)
+        asm volatile("bar.sync 1, %0;" ::"r"(T) : "memory");
+    else
+        asm volatile("bar.sync 2, %0;" ::"r"(T) : "memory");
 }
 
 // Codes of already scaled values (|v| <= Q up to one rounding), round to nearest even.
@@ -207,6 +225,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) eq_rmsnorm_kernel(const NormPa
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < E; ++k) sum = fmaf(h[k], h[k], sum);
+    float own = sum;  // this thread's squares, scaled where its values are
+    const bool scaled = !(own < kLargeSum);
+    if (scaled) {
+        own = 0.f;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            h[k] *= kScaleDown;
+            own = fmaf(h[k], h[k], own);
+        }
+    }
     // h becomes p = h gamma (absent columns stay 0)
     if (P.gamma) {
         if constexpr (MODE == kAligned) {
@@ -230,34 +258,59 @@ __global__ void __launch_bounds__(kMaxThreads, 1) eq_rmsnorm_kernel(const NormPa
         }
     }
     float top = 0.f;
-    if (narrow) {
+    const auto maximum = [&]() {
+        top = 0.f;
+        if (narrow) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) top = max_nan(top, fabsf(h[k]));
-    }
-    // sum and maximum over the row's T threads: warps, then the warps' results
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    }
-    if (T > 32) {
-        const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, warps = T / 32;
-        if (lane == 0) {
-            sum_s[warp] = sum;
-            max_s[warp] = top;
+            for (int k = 0; k < E; ++k) top = max_nan(top, fabsf(h[k]));
         }
-        __syncthreads();
-        const uint32_t first = sub * warps;
-        sum = lane < warps ? sum_s[first + lane] : 0.f;
-        top = lane < warps ? max_s[first + lane] : 0.f;
+    };
+    // sum and maximum over the row's T threads: warps, then the warps' results
+    const auto over_row = [&](bool again) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
             top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         }
+        if (T > 32) {
+            const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, warps = T / 32;
+            if (again) row_sync(sub, T);  // the first results have been read
+            if (lane == 0) {
+                sum_s[warp] = sum;
+                max_s[warp] = top;
+            }
+            if (again)
+                row_sync(sub, T);
+            else
+                __syncthreads();
+            const uint32_t first = sub * warps;
+            sum = lane < warps ? sum_s[first + lane] : 0.f;
+            top = lane < warps ? max_s[first + lane] : 0.f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            }
+        }
+    };
+    maximum();
+    over_row(false);
+    float eps = P.eps;
+    // A scaled thread's own sum is part of the row's, so this branch, the same for all of a row's threads, is
+    // taken wherever one has scaled its values.
+    if (!(sum < kLargeSum)) {
+        eps = eps * kScaleDown * kScaleDown;
+        if (!scaled) {
+            own = own * kScaleDown * kScaleDown;
+#pragma unroll
+            for (int k = 0; k < E; ++k) h[k] *= kScaleDown;
+        }
+        sum = own;
+        maximum();
+        over_row(true);
     }
     if (!live) return;
-    const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)P.cols) + P.eps);
+    const float rstd = __frsqrt_rn(__fdiv_rn(sum, (float)P.cols) + eps);
     if (!narrow) {
 #pragma unroll
         for (int k = 0; k < E; ++k) h[k] = __fmul_rn(h[k], rstd);

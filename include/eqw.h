@@ -426,8 +426,8 @@ EQW_API int eq_gemm_symbols_block(const eq_model *m, uint32_t layer, const void 
  *     out_scale[t] = fp32(fp32(m * rstd) / Q)
  * so out * out_scale is the normalised value; a token whose values are all
  * zero gets codes and scale 0, one with an infinity or a NaN the scale NaN.
- * Squares are summed in fp32: a row whose sum of squares passes the fp32
- * range comes out as zeros.
+ * A row whose sum of squares would pass the fp32 range is computed from h 2^-80
+ * (an exact scaling that cancels out), so any finite h gives finite results.
  * x, res, res_out and out are row-major with row strides in elements (>= cols);
  * any cols from 1 to 32768 and any element-aligned addresses (16-byte aligned
  * rows and cols % 8 == 0 take the vectorised accesses).  res_out may be res
