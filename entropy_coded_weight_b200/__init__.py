@@ -540,8 +540,9 @@ def gemv_w4(q, scales, x, y, group: int = 128, zeros=None, table=None, stream=No
 
     ``q`` uint8 [rows, cols / 2] holds two 4-bit codes per byte (the even column in the low half), ``scales``
     [rows, ceil(cols / group)] fp32, bf16 or fp16, ``x`` bf16 [tokens, cols] (rows may be strided), ``y`` fp32
-    [tokens, rows].  A code q stands for q - 8, for q - zeros[r, g] (``zeros`` uint8, like ``scales``), or for
-    ``table[q]`` (a CPU tensor of 16 bf16 values, read during the call).
+    [tokens, rows].  A code q stands for q - 8, for q - zeros[r, g] (``zeros`` uint8, like ``scales``, 0 to
+    127: a byte above makes its row's outputs NaN), or for ``table[q]`` (a CPU tensor of 16 bf16 values, read during
+    the call).
     """
     job = _w4_job(q, scales, x, y, group, zeros, table)
     st = _launch_stream(stream, q, scales, x, y, zeros)

@@ -1,7 +1,7 @@
 // Matrix-vector products with 4-bit weights and group scales: eq_gemv_w4.
 //
 //   y[t, r] = sum_g s[r, g] * sum_{c in group g} w(q[r, c]) * x[t, c],  t < tokens <= 32
-//   w(q) = q - 8, q - zero[r, g], or table[q] (16 bf16 values)
+//   w(q) = q - 8, q - zero[r, g] (0 to 127), or table[q] (16 bf16 values)
 // Every w is exact in bf16, so a group's inner sum runs on the tensor cores
 // (tcgen05.mma kind::f16, exact products, fp32 accumulator) and its scale
 // multiplies it once, in fp32, when the sum leaves tensor memory.
@@ -381,7 +381,10 @@ __global__ void __launch_bounds__(W4Shape<CODES, GB, TOK>::kThreads, 1)
                     if (NG > 1 && s_vec && size == 2) bits = (s_raw[j & ~1] >> (16 * (j & 1))) & 0xFFFFu;
                     s_now[j] = scale_value(bits, type);
                     zero[j] = 0x43084308u;
-                    if constexpr (CODES == kCodesZero) zero[j] = 0x43004300u | (z_raw >> (8 * j) & 15u) * 0x00010001u;
+                    if constexpr (CODES == kCodesZero) {  // bf16(128 + zero) is exact up to 127; more marks the sums
+                        zero[j] = 0x43004300u | (z_raw >> (8 * j) & 127u) * 0x00010001u;
+                        if (z_raw >> (8 * j) & 128u) s_now[j] = __uint_as_float(0x7FC00000u);
+                    }
                 }
                 if (k + kParts < k1) fetch(k + kParts);
                 if (!warp_wait(landed + 8 * slot, lap)) {

@@ -511,8 +511,10 @@ EQW_API int eq_gemm_symbols_a8_block(const eq_model *m, uint32_t layer, const vo
  * scale per group of 32, 64 or 128 consecutive columns of a row, for 1 to 32
  * tokens:
  *   y[t, r] = sum_g scale[r, g] * sum_{c in group g} w(q[r, c]) * x[t, c]
- *   w(q) = q - 8 (zeros NULL), q - zeros[r, g] (0..15), or table[q] (use_table;
+ *   w(q) = q - 8 (zeros NULL), q - zeros[r, g], or table[q] (use_table;
  *   16 finite values, EQ_ERR_INVALID_ARG otherwise)
+ * A zero point is a whole number from 0 to 127 (formats that store zero + 1 have
+ * 16); a byte above 127 makes its row's outputs NaN.
  * Products are exact, sums are fp32 in an order fixed by the shapes and
  * `tokens` (the result does not depend on timing).
  * q: [rows, cols / 2] bytes, row-major, column 2 i in the low half of byte i.
