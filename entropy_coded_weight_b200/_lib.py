@@ -120,6 +120,7 @@ SIGNATURES = {
     "eq_rmsnorm": (_i32, [_vp, _vp]),
     "eq_selftest_wait_timeout": (_i32, [_vp, _vp]),
     "eq_selftest_gemm_wait_timeout": (_i32, [_vp, _vp]),
+    "eq_selftest_a8_wait_timeout": (_i32, [_vp, _vp]),
     "eq_status_string": (ctypes.c_char_p, [_i32]),
     "eq_format_version": (_i32, []),
     "eq_build_checked": (_i32, []),

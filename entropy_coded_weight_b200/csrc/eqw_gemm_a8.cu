@@ -414,6 +414,73 @@ __device__ __forceinline__ uint32_t first_slab(uint32_t local, uint32_t t_tiles,
     return (local % t_tiles * 3 + local / t_tiles * 7) % slabs;
 }
 
+// The epilogue of a cluster's tiles: one of four warps, for its 32 accumulator lanes.  False when a wait ran out
+// here or elsewhere.  A warp that gives up still goes through its tiles, without waiting or storing: the four meet
+// at a barrier in every tile with super weights, however much later than the others one of them learns of it.
+template <int DT>
+__device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, uint32_t n_clusters, uint32_t rank,
+                                              uint32_t tmem, uint32_t done0, uint32_t free_c0,
+                                              const volatile uint32_t *abort, uint32_t warp, uint32_t lane) {
+    const uint32_t row = warp * 32u + lane;
+    bool ok = true;
+    uint32_t ti = 0;
+    for (uint32_t tile = cl, jb = 0; tile < P.total_units; tile += n_clusters) {
+        if (__any_sync(0xFFFFFFFFu, *abort != 0u)) ok = false;
+        while (jb + 1 < P.n_jobs && tile >= P.jobs[jb + 1].first_unit) ++jb;
+        const A8Job &J = P.jobs[jb];
+        const uint32_t local = tile - J.first_unit;
+        const uint32_t r = (local / P.t_tiles) * kPairRows + rank * kRowsTile + row;
+        const uint32_t m0 = (local % P.t_tiles) * kPairTok;
+        const float ws = r < J.rows ? J.ws[r] : 0.f;
+        if (J.n_out && local == 0 && warp == 0 && rank == 0) check_outliers(J, lane, 32, P.status);
+        const uint32_t segs = segments<DT>((J.cols + kSlab - 1) / kSlab);
+        for (uint32_t seg = 0; seg < segs && ok; ++seg, ++ti) {
+            const uint32_t a = ti & 1u;
+            if (!warp_wait(done0 + 8 * a, (ti >> 1) & 1u)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc0 = tmem + ((warp * 32u) << 16) + a * kPairTok;
+            const bool first = seg == 0, last = seg + 1 == segs;
+#pragma unroll 1
+            for (uint32_t c = 0; c < kPairTok && m0 + c < P.tokens; c += 32) {
+                uint32_t acc[32];
+                float xs[32];  // before the stores, which the compiler must take for stores to xs, too
+#pragma unroll
+                for (uint32_t j = 0; j < 32; ++j) xs[j] = J.xs[min(m0 + c + j, P.tokens - 1)];
+                tmem_ld32(acc0 + c, acc);
+                if (r >= J.rows) continue;
+                float *y = J.y + (size_t)(m0 + c) * J.rows + r;
+                if (first && last) {
+#pragma unroll
+                    for (uint32_t j = 0; j < 32; ++j) {
+                        const uint32_t t = m0 + c + j;
+                        if (t < P.tokens) y[(size_t)j * J.rows] = scaled<DT>(acc[j], xs[j], ws);
+                    }
+                } else {  // Y holds the sum of the segments so far (this thread's own stores) until the last one
+#pragma unroll
+                    for (uint32_t j = 0; j < 32; ++j) {
+                        const uint32_t t = m0 + c + j;
+                        if (t >= P.tokens) continue;
+                        float v = __uint_as_float(acc[j]);
+                        if (!first) v = __fadd_rn(y[(size_t)j * J.rows], v);
+                        y[(size_t)j * J.rows] = last ? scaled<EQ_E4M3>(__float_as_uint(v), xs[j], ws) : v;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(free_c0 + 8 * a);
+        }
+        if (J.n_out) {
+            epilogue_sync();  // the tile's Y is written
+            if (ok) add_outliers<DT>(J, r - row, m0, min(kPairTok, P.tokens - m0), 0, 1, row);
+        }
+    }
+    return ok;
+}
+
 template <int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
     eq_gemm_a8_pair_kernel(const __grid_constant__ A8Params P) {
@@ -531,64 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
                 if (!warp_wait(done0 + 8 * (k & 1u), (k >> 1) & 1u)) ok = false;
     } else if (warp < 4) {
         // ---- epilogue (both CTAs) ----
-        const uint32_t free_c0 = cluster_addr(free0, 0);
-        const uint32_t row = warp * 32u + lane;
-        uint32_t ti = 0;
-        for (uint32_t tile = cl, jb = 0; tile < P.total_units && ok; tile += n_clusters) {
-            if (__any_sync(0xFFFFFFFFu, abort_s != 0u)) break;
-            while (jb + 1 < P.n_jobs && tile >= P.jobs[jb + 1].first_unit) ++jb;
-            const A8Job &J = P.jobs[jb];
-            const uint32_t local = tile - J.first_unit;
-            const uint32_t r = (local / P.t_tiles) * kPairRows + rank * kRowsTile + row;
-            const uint32_t m0 = (local % P.t_tiles) * kPairTok;
-            const float ws = r < J.rows ? J.ws[r] : 0.f;
-            if (J.n_out && local == 0 && warp == 0 && rank == 0) check_outliers(J, lane, 32, P.status);
-            const uint32_t segs = segments<DT>((J.cols + kSlab - 1) / kSlab);
-            for (uint32_t seg = 0; seg < segs; ++seg, ++ti) {
-                const uint32_t a = ti & 1u;
-                if (!warp_wait(done0 + 8 * a, (ti >> 1) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t acc0 = tmem + ((warp * 32u) << 16) + a * kPairTok;
-                const bool first = seg == 0, last = seg + 1 == segs;
-#pragma unroll 1
-                for (uint32_t c = 0; c < kPairTok && m0 + c < P.tokens; c += 32) {
-                    uint32_t acc[32];
-                    float xs[32];  // before the stores, which the compiler must take for stores to xs, too
-#pragma unroll
-                    for (uint32_t j = 0; j < 32; ++j) xs[j] = J.xs[min(m0 + c + j, P.tokens - 1)];
-                    tmem_ld32(acc0 + c, acc);
-                    if (r >= J.rows) continue;
-                    float *y = J.y + (size_t)(m0 + c) * J.rows + r;
-                    if (first && last) {
-#pragma unroll
-                        for (uint32_t j = 0; j < 32; ++j) {
-                            const uint32_t t = m0 + c + j;
-                            if (t < P.tokens) y[(size_t)j * J.rows] = scaled<DT>(acc[j], xs[j], ws);
-                        }
-                    } else {  // Y holds the sum of the segments so far (this thread's own stores) until the last one
-#pragma unroll
-                        for (uint32_t j = 0; j < 32; ++j) {
-                            const uint32_t t = m0 + c + j;
-                            if (t >= P.tokens) continue;
-                            float v = __uint_as_float(acc[j]);
-                            if (!first) v = __fadd_rn(y[(size_t)j * J.rows], v);
-                            y[(size_t)j * J.rows] = last ? scaled<EQ_E4M3>(__float_as_uint(v), xs[j], ws) : v;
-                        }
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(free_c0 + 8 * a);
-            }
-            if (!ok) break;
-            if (J.n_out) {
-                epilogue_sync();  // the tile's Y is written
-                add_outliers<DT>(J, r - row, m0, min(kPairTok, P.tokens - m0), 0, 1, tid);
-            }
-        }
+        ok = pair_epilogue<DT>(P, cl, n_clusters, rank, tmem, done0, cluster_addr(free0, 0), &abort_s, warp, lane);
     }
     if (!ok) {
         abort_s = 1;
@@ -602,6 +612,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kPairTok) : "memory");
     }
 }
+
+// Failure-path check of the pair kernel's epilogue: its four warps on one tile of a job with super weights, whose
+// products are marked done.  Three of them store the tile and wait at its barrier; the last first runs out a bounded
+// wait on a barrier that nothing arrives on, raises the abort flag, and enters as a warp that has given up.  The
+// block has to end, with EQ_DEV_TIMEOUT set and its tensor memory freed.
+__global__ void __launch_bounds__(128, 1) eq_a8_wait_timeout_kernel(const __grid_constant__ A8Params P) {
+    __shared__ __align__(8) uint64_t never_s, done_s[2], free_s[2];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile uint32_t abort_s;
+    const uint32_t tid = threadIdx.x, warp = warp_index(), lane = tid & 31u;
+    const uint32_t never = smem_u32(&never_s), done0 = smem_u32(&done_s[0]), free0 = smem_u32(&free_s[0]);
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&tmem_base_s)), "r"(2 * kPairTok) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        mbar_init(never, 1);
+        for (uint32_t a = 0; a < 2; ++a) {
+            mbar_init(done0 + 8 * a, 1);
+            mbar_init(free0 + 8 * a, 8);
+        }
+        fence_mbar_init();
+        abort_s = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const uint32_t zero[16] = {};
+    tmem_st16(tmem + ((warp * 32u) << 16), zero);
+    tmem_st16(tmem + ((warp * 32u) << 16) + 16, zero);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncthreads();
+    bool ok = true;
+    if (warp == 0) warp_arrive(done0);
+    if (warp == 3 && !warp_wait(never, 0u)) {
+        ok = false;
+        abort_s = 1;
+        __syncwarp();
+    }
+    if (!pair_epilogue<EQ_INT8>(P, 0, 1, 0, tmem, done0, cluster_addr(free0, 0), &abort_s, warp, lane)) ok = false;
+    if (!ok) atomicOr(P.status, EQ_DEV_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kPairTok) : "memory");
+    }
+}
+__device__ uint32_t selftest_words[8];  // zeros: the job's scales, tokens, outputs and super weight
 
 int encode_map8(CUtensorMap *map, const void *p, uint32_t rows, uint32_t cols, uint32_t box_rows) {
     auto enc = tensor_map_encoder();
@@ -794,4 +856,21 @@ extern "C" EQW_API int eq_gemm_symbols_a8_block(const eq_model *m, uint32_t laye
     return a8_launch(jobs.data(), n, tokens, m->sm_limit, d_status, s);
 } catch (...) {
     return EQ_ERR_NOSPACE;
+}
+
+extern "C" EQW_API int eq_selftest_a8_wait_timeout(int32_t *d_status, cudaStream_t s) {
+    if (!d_status) return EQ_ERR_INVALID_ARG;
+    void *words = nullptr;
+    if (cudaGetSymbolAddress(&words, selftest_words) != cudaSuccess) return EQ_ERR_CUDA;
+    A8Params P{};
+    P.status = d_status;
+    P.tokens = P.t_tiles = P.n_jobs = P.total_units = 1;
+    A8Job &J = P.jobs[0];  // 1 x 16, one token, one super weight: all zero
+    J.ws = J.xs = J.out_val = static_cast<const float *>(words);
+    J.out_row = J.out_col = static_cast<const uint32_t *>(words);
+    J.x8 = static_cast<const uint8_t *>(words);
+    J.y = static_cast<float *>(words) + 7;
+    J.rows = J.n_out = J.out_stride = 1, J.cols = 16;
+    eq_a8_wait_timeout_kernel<<<1, 128, 0, s>>>(P);
+    return cudaGetLastError() == cudaSuccess ? EQ_OK : EQ_ERR_CUDA;
 }

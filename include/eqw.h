@@ -567,6 +567,15 @@ EQW_API int eq_build_checked(void);
  */
 EQW_API int eq_selftest_gemm_wait_timeout(int32_t *d_status, cudaStream_t s);
 
+/*
+ * The same check for the epilogue of eq_gemm_a8's pair kernel: one of its four
+ * warps gives up (on a barrier that nothing arrives on, after about a second)
+ * while the others wait for it at a tile's barrier; the block still ends, with
+ * EQ_DEV_TIMEOUT in *d_status and its TMEM freed.
+ * No fault, trap or hang.  Errors: EQ_ERR_INVALID_ARG, EQ_ERR_CUDA.
+ */
+EQW_API int eq_selftest_a8_wait_timeout(int32_t *d_status, cudaStream_t s);
+
 /* ---- misc ----------------------------------------------------------------------- */
 EQW_API const char *eq_status_string(int status);
 
