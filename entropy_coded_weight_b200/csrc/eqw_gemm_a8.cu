@@ -160,8 +160,11 @@ __device__ __noinline__ void add_outliers(const A8Job &J, uint32_t n0, uint32_t 
     }
 }
 
-// The four epilogue warps.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four epilogue warps, each as a whole.
+__device__ __forceinline__ void epilogue_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+}
 
 // Reports super weights outside their matrix or out of order: entries first, first + step, ...
 __device__ __forceinline__ void check_outliers(const A8Job &J, uint32_t first, uint32_t step, int32_t *status) {
@@ -286,6 +289,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
                 float xs[16];  // before the stores, which the compiler must take for stores to xs, too
 #pragma unroll
                 for (uint32_t j = 0; j < 16; ++j) xs[j] = J.xs[m0 + min(c + j, toks - 1)];
+                __syncwarp();  // rows past the end skip the stores below
                 tmem_ld16(lane_base + c, acc);
                 if (r < J.rows) {
 #pragma unroll
@@ -449,6 +453,7 @@ __device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, ui
                 float xs[32];  // before the stores, which the compiler must take for stores to xs, too
 #pragma unroll
                 for (uint32_t j = 0; j < 32; ++j) xs[j] = J.xs[min(m0 + c + j, P.tokens - 1)];
+                __syncwarp();  // the load is one instruction of the whole warp; rows past the end left the others' stores
                 tmem_ld32(acc0 + c, acc);
                 if (r >= J.rows) continue;
                 float *y = J.y + (size_t)(m0 + c) * J.rows + r;
