@@ -144,7 +144,9 @@ __device__ __noinline__ void add_outliers(const A8Job &J, uint32_t n0, uint32_t 
             uint32_t o = from + id / count;
             const uint32_t i = id % count, c = 4 * (first + step * (i / 4)) + i % 4, t = m0 + c;
             const uint32_t r = J.out_row[(size_t)o * J.out_stride];
-            if (c >= toks || r >= J.rows || (o > lo && J.out_row[(size_t)(o - 1) * J.out_stride] == r)) continue;
+            // entries out of order may bring rows of other tiles here, whose outputs other CTAs write
+            if (c >= toks || r >= J.rows || r - n0 >= kRowsTile) continue;
+            if (o > lo && J.out_row[(size_t)(o - 1) * J.out_stride] == r) continue;  // counted with the first
             const float sc = J.xs[t];
             float sum = 0.f;
             for (; o < hi && J.out_row[(size_t)o * J.out_stride] == r; ++o) {

@@ -470,7 +470,7 @@ EQW_API int eq_rmsnorm(const eq_rmsnorm_args *a, cudaStream_t s);
  * Super weights: n_out entries sorted by row, as three arrays whose entries are
  * out_stride elements apart (1: plain arrays, 3: the container's records); one
  * outside the matrix is skipped and reported (EQ_DEV_BAD_OUTLIER), entries out
- * of order are reported and may be missed.  They are meant to be few: a row's
+ * of order are reported and may be missed (nothing else about Y changes).  They are meant to be few: a row's
  * are added one after the other, by as many threads as there are tokens.
  * The jobs may have different shapes and types and may share x8, but write
  * different y.  One launch per 8 jobs of a type; nothing is launched when one
