@@ -48,6 +48,7 @@ constexpr uint32_t kA8Threads = 192;                     // 4 epilogue warps, th
 constexpr uint32_t kMaxSplit = 8;
 constexpr uint32_t kMaxRows = 0x7FFFFF00u;               // tensor-map coordinates are 32-bit signed
 constexpr uint32_t kMaxInt8Cols = 131056;                // 128 * 128 * cols < 2^31
+constexpr uint32_t kMaxE4m3Cols = 1u << 26;              // 2^19 slabs x 5462 parts of K (kMaxChain): 32-bit products
 // E4M3: the tensor core rounds its accumulator towards zero at every step, an error that grows with K (relative
 // 5e-7 of the result's norm at 64 slabs, 2.5e-6 at 224, against 1.3e-7 for fp32 products summed in order).  So at
 // most this many slabs go into one accumulator, and the accumulators' values are added in fp32.
@@ -410,6 +411,8 @@ __device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map
 }
 
 // The parts of a tile's K that go through an accumulator of their own (kMaxChain).
+static_assert((uint64_t)(kMaxE4m3Cols / kSlab) * ((kMaxE4m3Cols / kSlab + kMaxChain - 1) / kMaxChain) <= 0xFFFFFFFFull,
+              "slab numbers of the parts");
 template <int DT>
 __device__ __forceinline__ uint32_t segments(uint32_t slabs) {
     return DT == EQ_INT8 ? 1u : (slabs + kMaxChain - 1) / kMaxChain;
@@ -689,7 +692,7 @@ int check_job(const eq_a8_job &j, uint32_t tokens) {
     if (j.dtype != EQ_INT8 && j.dtype != EQ_E4M3) return EQ_ERR_INVALID_ARG;
     if (!j.rows) return EQ_OK;
     if (j.rows > kMaxRows) return EQ_ERR_UNSUPPORTED;
-    if (!j.cols || j.cols % 16 || (j.dtype == EQ_INT8 && j.cols > kMaxInt8Cols)) return EQ_ERR_UNSUPPORTED;
+    if (!j.cols || j.cols % 16 || j.cols > (j.dtype == EQ_INT8 ? kMaxInt8Cols : kMaxE4m3Cols)) return EQ_ERR_UNSUPPORTED;
     if (!j.sym || !j.scale || (tokens && (!j.x8 || !j.x_scale || !j.y))) return EQ_ERR_INVALID_ARG;
     const auto at = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
     if (at(j.sym) % 16 || at(j.x8) % 16 || at(j.scale) % 4 || at(j.x_scale) % 4 || at(j.y) % 4)

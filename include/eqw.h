@@ -465,8 +465,8 @@ EQW_API int eq_rmsnorm(const eq_rmsnorm_args *a, cudaStream_t s);
  * eq_decode_symbols writes.  Int8: S is exact.  E4M3: exact products summed in
  * fp32 in a fixed order.  The results of one call do not depend on timing, but
  * the order of an E4M3 sum does depend on tokens, rows and cols.
- * Needs cols % 16 == 0, cols > 0, and cols <= 131056 for Int8 (EQ_ERR_UNSUPPORTED
- * otherwise); at most 2^31 - 256 rows and tokens.  sym and x8 16-byte aligned, contiguous rows.
+ * Needs cols % 16 == 0, cols > 0, and cols <= 131056 for Int8, 2^26 for E4M3
+ * (EQ_ERR_UNSUPPORTED otherwise); at most 2^31 - 256 rows and tokens.  sym and x8 16-byte aligned, contiguous rows.
  * Super weights: n_out entries sorted by row, as three arrays whose entries are
  * out_stride elements apart (1: plain arrays, 3: the container's records); one
  * outside the matrix is skipped and reported (EQ_DEV_BAD_OUTLIER), entries out

@@ -1,0 +1,40 @@
+"""Limits of the 8-bit GEMM's arguments: no GPU and no launch (every call is refused or empty)."""
+import pytest
+
+FAKE = 0x7F0000000000  # 256-byte aligned device-looking address; never dereferenced
+OK, INVALID, UNSUPPORTED = 0, 1, 3
+INT8, E4M3 = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from entropy_coded_weight_b200 import build
+    build.build()
+    from entropy_coded_weight_b200 import _lib
+    return _lib
+
+
+def _call(lib, tokens, **kw):
+    a = dict(sym=FAKE, scale=FAKE, x8=FAKE, x_scale=FAKE, y=FAKE, out_row=None, out_col=None, out_val=None, rows=128,
+             cols=64, dtype=E4M3, n_out=0, out_stride=0)
+    a.update(kw)
+    return lib.load().eq_gemm_a8((lib.eq_a8_job * 1)(lib.eq_a8_job(**a)), 1, tokens, FAKE, None)
+
+
+@pytest.mark.parametrize("cols,code", [(1 << 26, OK), ((1 << 26) + 16, UNSUPPORTED), (642000 * 128, UNSUPPORTED),
+                                       (1 << 31, UNSUPPORTED), ((1 << 32) - 16, UNSUPPORTED)])
+def test_e4m3_columns(lib, cols, code):
+    """Beyond 2^26 columns the numbers of slabs and parts of K pass 32 bits: the kernel would wait for slabs that
+    never come, or skip some."""
+    assert _call(lib, 0, cols=cols) == code
+    assert _call(lib, 0, cols=cols, dtype=INT8) == UNSUPPORTED
+
+
+def test_parts_of_k_within_32_bits():
+    """The kernel's split of the slabs into parts, in 32 bits and without a limit, at the widest accepted matrix."""
+    for cols in ((1 << 26), (1 << 26) - 16, 12288, 12304, 28672):
+        slabs = -(-cols // 128)
+        segs = -(-slabs // 96)
+        wide = [slabs * s // segs for s in range(segs + 1)]
+        assert wide == [((slabs * s) & 0xFFFFFFFF) // segs for s in range(segs + 1)]
+        assert all(0 < b - a <= 96 for a, b in zip(wide, wide[1:])) and wide[-1] == slabs
