@@ -354,12 +354,13 @@ def gemv_bf16(w, x, y, stream=None) -> None:
 # ---- activation and 4-bit operators ------------------------------------------------------
 # These run once per layer and decoded token, so their checks are written for few Python steps.
 _TYPES: dict = {}  # torch dtype -> EQ_* element type
-_device = _raw_stream = None
+_device = _raw_stream = _bytes = None
 
 
 def _setup() -> None:
-    global _device, _raw_stream
+    global _device, _raw_stream, _bytes
     import torch
+    _bytes = torch.uint8
     _TYPES.update({torch.bfloat16: EQ_BF16, torch.float32: EQ_F32, torch.float16: EQ_F16, torch.int8: EQ_INT8,
                    torch.float8_e4m3fn: EQ_E4M3})
     _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -460,6 +461,8 @@ def _a8_job(sym, scale, x8, x_scale, y, outliers) -> bytes:
     rows, cols = sym.shape
     dtype = _type(x8)
     _check_a8(rows, cols, dtype, sym, x8, x_scale, y)
+    if sym.dtype != x8.dtype and sym.dtype != _bytes:
+        raise ValueError("sym must be uint8 (the decoder's bytes) or of x8's dtype")
     if _type(scale) != EQ_F32 or scale.numel() != rows or not scale.is_contiguous():
         raise ValueError("scale must be fp32 [rows], contiguous")
     rp = cp = vp = n_out = 0
@@ -479,9 +482,9 @@ def gemm_a8(sym, scale, x8, x_scale, y, status, outliers=None, stream=None) -> N
     """eq_gemm_a8 for one matrix given by its decoded symbols: y[t, r] = scale[r] * x_scale[t] * sum_c x8[t, c] *
     sym[r, c] (+ super weights).
 
-    ``sym`` [rows, cols] holds Int8 or E4M3 bytes (``Model.decode_symbols``), ``x8`` [tokens, cols] int8 or
-    float8_e4m3fn codes of the same type (``rmsnorm``), ``scale`` fp32 [rows], ``x_scale`` fp32 [tokens],
-    ``y`` fp32 [tokens, rows].  ``outliers``: (row, col, value) tensors (int32, int32, fp32) sorted by row.
+    ``sym`` [rows, cols] holds Int8 or E4M3 symbols, as bytes (uint8, ``Model.decode_symbols``) or typed like
+    ``x8`` [tokens, cols], whose dtype, int8 or float8_e4m3fn, is taken for both (``rmsnorm``); ``scale`` fp32
+    [rows], ``x_scale`` fp32 [tokens], ``y`` fp32 [tokens, rows].  ``outliers``: (row, col, value) tensors (int32, int32, fp32) sorted by row.
     """
     job = _a8_job(sym, scale, x8, x_scale, y, outliers)
     st = _launch_stream(stream, sym, scale, x8, x_scale, y, status)

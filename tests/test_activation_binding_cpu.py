@@ -1,0 +1,41 @@
+"""What the Python entry points of the activation and 4-bit operators refuse: no GPU, no launch."""
+import pytest
+import torch
+
+import entropy_coded_weight_b200 as E
+
+
+@pytest.fixture
+def reach(monkeypatch):
+    """CPU tensors get as far as the library call, which is recorded instead of made."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(E, "_launch_stream", lambda *a: 0)
+    monkeypatch.setattr(E, "load", lambda: Lib())
+    return calls
+
+
+def _a8(sym_dtype, x_dtype):
+    return dict(sym=torch.zeros(8, 32, dtype=sym_dtype), scale=torch.ones(8), x8=torch.zeros(2, 32, dtype=x_dtype),
+                x_scale=torch.ones(2), y=torch.zeros(2, 8), status=torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("x_dtype", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("sym_dtype", [torch.uint8, torch.int8, torch.float8_e4m3fn, torch.bool, torch.float8_e5m2])
+def test_symbols_are_bytes_or_typed_like_the_tokens(reach, sym_dtype, x_dtype):
+    a = _a8(sym_dtype, x_dtype)
+    lists = [[a[k]] for k in ("sym", "scale", "x8", "x_scale", "y")]
+    if sym_dtype in (torch.uint8, x_dtype):
+        E.gemm_a8(**a)
+        E.gemm_a8_block(*lists, a["status"])
+        assert reach == ["eq_gemm_a8"] * 2
+        return
+    with pytest.raises(ValueError):
+        E.gemm_a8(**a)
+    with pytest.raises(ValueError):
+        E.gemm_a8_block(*lists, a["status"])
+    assert not reach
