@@ -305,6 +305,7 @@ class Model:
         fp32 [tokens], y fp32 [tokens, rows]."""
         info = self.info(matrix)
         tokens = _check_a8(info.rows, info.cols, info.dtype, sym, x8, x_scale, y)
+        _check_status(status)
         st = _launch_stream(stream, sym, x8, x_scale, y, status)
         check(self._L.eq_gemm_symbols_a8(self._m, matrix, sym.data_ptr(), x8.data_ptr(), x_scale.data_ptr(),
                                          tokens, y.data_ptr(), status.data_ptr(), st), "eq_gemm_symbols_a8")
@@ -322,6 +323,7 @@ class Model:
             if x8s[i].shape[0] != tokens:
                 raise ValueError("every input of a block GEMM takes the same number of tokens")
             _check_a8(info.rows, info.cols, info.dtype, syms[i], x8s[i], x_scales[i], ys[i])
+        _check_status(status)
         st = _launch_stream(stream, status, *syms, *x8s, *x_scales, *ys)
 
         def ptrs(ts):
@@ -440,6 +442,11 @@ def rmsnorm(x, out, gamma=None, eps: float = 1e-6, residual=None, residual_out=N
                                               cols, _type(x), rt, ot, eps), st), "eq_rmsnorm")
 
 
+def _check_status(status) -> None:
+    if status.element_size() != 4 or status.is_floating_point() or not status.numel():
+        raise ValueError("status must be an int32 tensor of at least one element")
+
+
 def _check_a8(rows: int, cols: int, dtype: int, sym, x8, x_scale, y) -> int:
     """Shapes and types of an 8-bit product's tensors; the number of tokens."""
     shape = x8.shape
@@ -487,6 +494,7 @@ def gemm_a8(sym, scale, x8, x_scale, y, status, outliers=None, stream=None) -> N
     [rows], ``x_scale`` fp32 [tokens], ``y`` fp32 [tokens, rows].  ``outliers``: (row, col, value) tensors (int32, int32, fp32) sorted by row.
     """
     job = _a8_job(sym, scale, x8, x_scale, y, outliers)
+    _check_status(status)
     st = _launch_stream(stream, sym, scale, x8, x_scale, y, status)
     check(load().eq_gemm_a8(job, 1, x8.shape[0], status.data_ptr(), st), "eq_gemm_a8")
 
@@ -504,6 +512,7 @@ def gemm_a8_block(syms, scales, x8s, x_scales, ys, status, outliers=None, stream
         raise ValueError("every input of a block GEMM takes the same number of tokens")
     jobs = b"".join(_a8_job(syms[i], scales[i], x8s[i], x_scales[i], ys[i], None if outliers is None else outliers[i])
                     for i in range(n))
+    _check_status(status)
     st = _launch_stream(stream, status, *syms, *scales, *x8s, *x_scales, *ys)
     check(load().eq_gemm_a8(jobs, n, tokens, status.data_ptr(), st), "eq_gemm_a8")
 

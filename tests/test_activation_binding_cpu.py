@@ -39,3 +39,34 @@ def test_symbols_are_bytes_or_typed_like_the_tokens(reach, sym_dtype, x_dtype):
     with pytest.raises(ValueError):
         E.gemm_a8_block(*lists, a["status"])
     assert not reach
+
+
+@pytest.mark.parametrize("status", [torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int8),
+                                    torch.zeros(1, dtype=torch.int64), torch.zeros(1), torch.zeros(2, dtype=torch.int16)])
+def test_status_is_a_word(reach, status):
+    """On an error the kernels OR four bytes into it."""
+    a = {**_a8(torch.uint8, torch.int8), "status": status}
+    lists = [[a[k]] for k in ("sym", "scale", "x8", "x_scale", "y")]
+
+    class Info:
+        rows, cols, dtype = 8, 32, E.EQ_INT8
+
+    class Fake:
+        _L, _m = E.load(), None
+
+        def info(self, matrix):
+            return Info
+
+        def layer_matrices(self, layer):
+            return [0]
+
+    m = [[a[k]] for k in ("sym", "x8", "x_scale", "y")]
+    for call in (lambda st: E.gemm_a8(**{**a, "status": st}), lambda st: E.gemm_a8_block(*lists, st),
+                 lambda st: E.Model.gemm_symbols_a8(Fake(), 0, *(v[0] for v in m), st),
+                 lambda st: E.Model.gemm_symbols_a8_block(Fake(), 0, *m, st)):
+        n = len(reach)
+        with pytest.raises(ValueError):
+            call(status)
+        assert len(reach) == n
+        call(torch.zeros(1, dtype=torch.int32))
+        assert len(reach) == n + 1
