@@ -390,6 +390,9 @@ def _launch_stream(stream, *tensors) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_MAX_U32 = 0xFFFFFFFF  # what the library takes sizes in; ctypes would cut a larger one without a word
+
+
 def _rows(t, what: str, shape) -> int:
     """Row stride in elements of a [tokens, cols] tensor whose columns are adjacent."""
     if t.shape == shape:
@@ -414,6 +417,8 @@ def rmsnorm(x, out, gamma=None, eps: float = 1e-6, residual=None, residual_out=N
     if len(shape) != 2:
         raise ValueError("x must be [tokens, cols]")
     tokens, cols = shape
+    if tokens > _MAX_U32 or cols > _MAX_U32:
+        raise ValueError("x has more than 2^32 - 1 tokens or columns")
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs residual")
@@ -453,6 +458,8 @@ def _check_a8(rows: int, cols: int, dtype: int, sym, x8, x_scale, y) -> int:
     if len(shape) != 2 or shape[1] != cols or not x8.is_contiguous() or _type(x8) != dtype:
         raise ValueError("x8 must be [tokens, cols], contiguous, int8 or float8_e4m3fn like the symbols")
     tokens = shape[0]
+    if tokens > _MAX_U32 or rows > _MAX_U32 or cols > _MAX_U32:
+        raise ValueError("more than 2^32 - 1 tokens, rows or columns")
     if sym.element_size() != 1 or sym.numel() < rows * cols or not sym.is_contiguous():
         raise ValueError("sym must hold rows * cols bytes, contiguous")
     if _type(x_scale) != EQ_F32 or x_scale.numel() != tokens or not x_scale.is_contiguous():
@@ -527,6 +534,8 @@ def _w4_job(q, scales, x, y, group: int, zeros, table) -> bytes:
     rows, cols = qs[0], 2 * qs[1]
     if x.dim() != 2 or _type(x) != EQ_BF16:
         raise ValueError("x must be bf16 [tokens, cols]")
+    if x.shape[0] > _MAX_U32 or rows > _MAX_U32 or cols > _MAX_U32:
+        raise ValueError("more than 2^32 - 1 tokens, rows or columns")
     xs = _rows(x, "x", (x.shape[0], cols))
     n = rows * -(-cols // group) if group > 0 else -1
     if scales.numel() != n or not scales.is_contiguous():

@@ -70,3 +70,30 @@ def test_status_is_a_word(reach, status):
         assert len(reach) == n
         call(torch.zeros(1, dtype=torch.int32))
         assert len(reach) == n + 1
+
+
+BIG = 2 ** 32 + 1
+
+
+def test_sizes_beyond_32_bits(reach):
+    """2^32 + 1 tokens would arrive as one (every tensor here is empty or one row seen many times)."""
+    none = torch.empty(0, 0, dtype=torch.uint8)
+    meta = {k: torch.empty(BIG, device="meta") for k in ("x_scale", "out_scale")}
+    a8 = dict(sym=none, scale=torch.empty(0), x8=torch.empty(BIG, 0, dtype=torch.int8), x_scale=meta["x_scale"],
+              y=torch.empty(BIG, 0), status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        E.gemm_a8(**a8)
+    with pytest.raises(ValueError):
+        E.gemm_a8_block(*([a8[k]] for k in ("sym", "scale", "x8", "x_scale", "y")), a8["status"])
+    q, s = torch.empty(0, 16, dtype=torch.uint8), torch.empty(0, 1)
+    x = torch.zeros(1, 32, dtype=torch.bfloat16).expand(BIG, 32)
+    y = torch.empty(BIG, 0)
+    with pytest.raises(ValueError):
+        E.gemv_w4(q, s, x, y, group=32)
+    with pytest.raises(ValueError):
+        E.gemv_w4_block([q], [s], [x], [y], group=32)
+    with pytest.raises(ValueError):
+        E.rmsnorm(torch.empty(BIG, 0), torch.empty(BIG, 0, dtype=torch.int8), out_scale=meta["out_scale"])
+    with pytest.raises(ValueError):
+        E.rmsnorm(torch.empty(0, BIG), torch.empty(0, BIG, dtype=torch.bfloat16))
+    assert not reach
