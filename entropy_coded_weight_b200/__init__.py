@@ -306,7 +306,7 @@ class Model:
         info = self.info(matrix)
         tokens = _check_a8(info.rows, info.cols, info.dtype, sym, x8, x_scale, y)
         _check_status(status)
-        st = _launch_stream(stream, sym, x8, x_scale, y, status)
+        st = _launch_stream(stream, sym, x8, x_scale, y, status, self.d_blob)
         check(self._L.eq_gemm_symbols_a8(self._m, matrix, sym.data_ptr(), x8.data_ptr(), x_scale.data_ptr(),
                                          tokens, y.data_ptr(), status.data_ptr(), st), "eq_gemm_symbols_a8")
 
@@ -324,7 +324,7 @@ class Model:
                 raise ValueError("every input of a block GEMM takes the same number of tokens")
             _check_a8(info.rows, info.cols, info.dtype, syms[i], x8s[i], x_scales[i], ys[i])
         _check_status(status)
-        st = _launch_stream(stream, status, *syms, *x8s, *x_scales, *ys)
+        st = _launch_stream(stream, status, self.d_blob, *syms, *x8s, *x_scales, *ys)
 
         def ptrs(ts):
             return (ctypes.c_void_p * max(1, n))(*(t.data_ptr() for t in ts))

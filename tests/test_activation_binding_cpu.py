@@ -52,7 +52,7 @@ def test_status_is_a_word(reach, status):
         rows, cols, dtype = 8, 32, E.EQ_INT8
 
     class Fake:
-        _L, _m = E.load(), None
+        _L, _m, d_blob = E.load(), None, None
 
         def info(self, matrix):
             return Info
@@ -97,3 +97,54 @@ def test_sizes_beyond_32_bits(reach):
     with pytest.raises(ValueError):
         E.rmsnorm(torch.empty(0, BIG), torch.empty(0, BIG, dtype=torch.bfloat16))
     assert not reach
+
+
+def test_the_model_is_on_the_current_device(monkeypatch):
+    """The kernels read scales and super weights from the model's own bytes: a model on another device than the
+    current one is refused like any other tensor there."""
+    class On:
+        """A tensor on device `dev`, as far as the check of devices looks."""
+        def __init__(self, t, dev):
+            self.t, self.dev, self.device = t, dev, f"cuda:{dev}"
+
+        def get_device(self):
+            return self.dev
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    class Info:
+        rows, cols, dtype = 8, 32, E.EQ_INT8
+
+    class Fake:
+        _m = None
+
+        def __init__(self, dev):
+            self.d_blob, self.called = On(torch.zeros(1), dev), []
+            self._L = self
+
+        def info(self, matrix):
+            return Info
+
+        def layer_matrices(self, layer):
+            return [0]
+
+        def eq_gemm_symbols_a8(self, *a):
+            return self.called.append(1) or 0
+
+        eq_gemm_symbols_a8_block = eq_gemm_symbols_a8
+
+    E._type(torch.zeros(1))  # sets the dtype table up before the device query is replaced
+    monkeypatch.setattr(E, "_device", lambda: 1)
+    monkeypatch.setattr(E, "_raw_stream", lambda dev: 0)
+    a = {k: On(v, 1) for k, v in _a8(torch.uint8, torch.int8).items()}
+    m = [a[k] for k in ("sym", "x8", "x_scale", "y")]
+    for call in (lambda f: E.Model.gemm_symbols_a8(f, 0, *m, a["status"]),
+                 lambda f: E.Model.gemm_symbols_a8_block(f, 0, *([v] for v in m), a["status"])):
+        f = Fake(1)
+        call(f)
+        assert f.called
+        f = Fake(0)
+        with pytest.raises(ValueError):
+            call(f)
+        assert not f.called
