@@ -603,5 +603,5 @@ def selftest_gemm_wait_timeout(status, stream=None) -> None:
 
 def selftest_a8_wait_timeout(status, stream=None) -> None:
     """eq_selftest_a8_wait_timeout: one epilogue warp of the 8-bit GEMM's pair kernel gives up (about a second) while
-    the other three wait for it; the block ORs EQ_DEV_TIMEOUT into ``status``, frees its TMEM and ends."""
+    the other seven wait for it; the block ORs EQ_DEV_TIMEOUT into ``status``, frees its TMEM and ends."""
     check(load().eq_selftest_a8_wait_timeout(status.data_ptr(), _stream_handle(stream)), "eq_selftest_a8_wait_timeout")

@@ -44,15 +44,19 @@ constexpr uint32_t kMmaK8 = 32;                          // K per tcgen05.mma on
 constexpr uint32_t kAtom = 8 * kSlab;                    // 8-row swizzle atom (SBO)
 constexpr uint32_t kWTile = kRowsTile * kSlab;           // 16 KB of symbols per stage
 constexpr uint32_t kMaxA8Jobs = 8;  // (kernel parameters: 4 KB)
-constexpr uint32_t kA8Threads = 192;                     // 4 epilogue warps, the loader warp, the MMA warp
+constexpr uint32_t kA8Threads = 192;                     // split: 4 epilogue warps, the loader warp, the MMA warp
+constexpr uint32_t kPairThreads = 320;                   // pairs: 8 epilogue warps, the loader warp, the MMA warp
+constexpr uint32_t kPairEpilogue = 256;                  // their threads
 constexpr uint32_t kMaxSplit = 8;
 constexpr uint32_t kMaxRows = 0x7FFFFF00u;               // tensor-map coordinates are 32-bit signed
 constexpr uint32_t kMaxInt8Cols = 131056;                // 128 * 128 * cols < 2^31
-constexpr uint32_t kMaxE4m3Cols = 1u << 26;              // 2^19 slabs x 5462 parts of K (kMaxChain): 32-bit products
-// E4M3: the tensor core rounds its accumulator towards zero at every step, an error that grows with K (relative
-// 5e-7 of the result's norm at 64 slabs, 2.5e-6 at 224, against 1.3e-7 for fp32 products summed in order).  So at
-// most this many slabs go into one accumulator, and the accumulators' values are added in fp32.
-constexpr uint32_t kMaxChain = 96;
+constexpr uint32_t kMaxE4m3Cols = 1u << 26;              // far inside 32-bit slab numbers and coordinates
+// E4M3: the tensor core rounds its accumulator towards zero at every step, so a chain's error is a bias that grows
+// with its length. Relative to the result's norm, one accumulator for all of K: 2.3e-7 at 32 slabs, 5.0e-7 at 64, 2.5e-6
+// at 224; fp32 products summed in order by a library: 0.9e-7, 1.3e-7, 2.8e-7. So K is cut into chains with an
+// accumulator each, whose values are added in fp32, rounded to nearest: with chains of 16 slabs 1.2e-7 to 1.4e-7 at
+// any K. A split CTA that has no tensor memory for as many accumulators takes chains of up to twice that.
+constexpr uint32_t kChain = 16;
 
 // Instruction descriptor: 8-bit K-major operands, N tokens, M rows.
 template <int DT>
@@ -85,7 +89,8 @@ struct A8Params {
     int32_t *status;
     uint32_t tokens, t_tiles, n_jobs, total_units;
     uint32_t tok;             // split kernel: tokens per tile (a multiple of 16), its stages and their size,
-    uint32_t stages, stage_bytes, tmem_cols;  // and the accumulator's columns
+    uint32_t stages, stage_bytes, tmem_cols;  // and the accumulators' columns
+    uint32_t accs;            // accumulators that share a CTA's K (E4M3)
     A8Job jobs[kMaxA8Jobs];
 };
 static_assert(sizeof(A8Params) <= 4096, "kernel parameter space");
@@ -129,19 +134,19 @@ __device__ __forceinline__ uint32_t first_outlier(const A8Job &J, uint32_t r) {
 }
 
 // Y[t, r] += sum of bf16(v) * xs[t] * x8[t, c] over the super weights of rows [n0, n0 + 128), for this CTA's
-// tokens: count of them, the i-th is 4 (first + step (i / 4)) + i % 4 from m0 on, up to toks.  The 128
-// epilogue threads share the (row, token) pairs; each output has one writer.  The stores that wrote Y
-// have been ordered before by a barrier.
+// tokens: count of them, the i-th is 4 (first + step (i / 4)) + i % 4 from m0 on, up to toks.  The epilogue's
+// threads share the (row, token) pairs; each output has one writer.  The stores that wrote Y have been
+// ordered before by a barrier.
 template <int DT>
 __device__ __noinline__ void add_outliers(const A8Job &J, uint32_t n0, uint32_t m0, uint32_t toks, uint32_t first,
-                                          uint32_t step, uint32_t tid) {
+                                          uint32_t step, uint32_t tid, uint32_t threads) {
     const uint32_t lo = first_outlier(J, n0), hi = first_outlier(J, n0 + kRowsTile);
     if (lo == hi) return;
     const uint32_t chunks = first * 4 < toks ? ((toks + 3) / 4 - first + step - 1) / step : 0, count = chunks * 4;
     constexpr uint32_t kMost = 1u << 20;  // entries at a time: their (entry, token) pairs have 32-bit numbers
     for (uint32_t from = lo; from < hi; from += min(hi - from, kMost)) {
         const uint32_t pairs = min(hi - from, kMost) * count;
-        for (uint32_t id = tid; id < pairs; id += 128) {
+        for (uint32_t id = tid; id < pairs; id += threads) {
             uint32_t o = from + id / count;
             const uint32_t i = id % count, c = 4 * (first + step * (i / 4)) + i % 4, t = m0 + c;
             const uint32_t r = J.out_row[(size_t)o * J.out_stride];
@@ -163,10 +168,11 @@ __device__ __noinline__ void add_outliers(const A8Job &J, uint32_t n0, uint32_t 
     }
 }
 
-// The four epilogue warps, each as a whole.
+// The epilogue's warps, each as a whole.
+template <int THREADS>
 __device__ __forceinline__ void epilogue_sync() {
     __syncwarp();
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // Reports super weights outside their matrix or out of order: entries first, first + step, ...
@@ -198,6 +204,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
     const uint32_t n0 = (local / P.t_tiles) * kRowsTile, m0 = (local % P.t_tiles) * TT;
     const uint32_t slabs = (J.cols + kSlab - 1) / kSlab;  // >= parts (host)
     const uint32_t k0 = (uint32_t)((uint64_t)slabs * rank / parts), k1 = (uint32_t)((uint64_t)slabs * (rank + 1) / parts);
+    const uint32_t accs = DT == EQ_INT8 ? 1u : min(P.accs, k1 - k0);
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -253,7 +260,12 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
         uint32_t st = 0, ph = 0;
         const uint32_t idesc = instr_desc<DT>(TT, kRowsTile);
         const uint64_t a0 = slab_desc(base), b0 = slab_desc(base + kWTile);
+        uint32_t acc = 0, from = k0, to = k0 + (k1 - k0) / accs;  // this accumulator's slabs
         for (uint32_t k = k0; k < k1; ++k) {
+            if (k == to) {
+                ++acc;
+                from = to, to = k0 + (k1 - k0) * (acc + 1) / accs;
+            }
             if (!warp_wait(full0 + 8 * st, ph)) {
                 ok = false;
                 break;
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
                 const uint64_t off = (uint64_t)((st * stage_bytes) >> 4);
 #pragma unroll
                 for (uint32_t kk = 0; kk < kSlab / kMmaK8; ++kk)  // K step: 32 bytes, 2 descriptor units
-                    mma8<DT>(tmem, a0 + off + 2u * kk, b0 + off + 2u * kk, idesc, (k - k0) | kk);
+                    mma8<DT>(tmem + acc * TT, a0 + off + 2u * kk, b0 + off + 2u * kk, idesc, (k - from) | kk);
                 tc_commit(empty0 + 8 * st);
                 if (k + 1 == k1) tc_commit(done);
             }
@@ -283,6 +295,20 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
     if (!ok) atomicOr(P.status, EQ_DEV_TIMEOUT);
     __syncwarp();
     const uint32_t lane_base = tmem + ((warp * 32u) << 16);
+    const auto load_sums = [&](uint32_t c, uint32_t (&v)[16]) {  // 16 tokens' sums of the accumulators, in order
+        __syncwarp();  // rows past the end skip what the others' lanes do with them
+        tmem_ld16(lane_base + c, v);
+        if constexpr (DT == EQ_E4M3) {
+#pragma unroll 1
+            for (uint32_t a = 1; a < accs; ++a) {
+                uint32_t more[16];
+                tmem_ld16(lane_base + a * TT + c, more);
+#pragma unroll
+                for (uint32_t j = 0; j < 16; ++j)
+                    v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(more[j])));
+            }
+        }
+    };
     const uint32_t toks = min(TT, P.tokens - m0);  // of this tile
     if (parts == 1) {
         if (warp < 4 && ok) {
@@ -292,8 +318,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
                 float xs[16];  // before the stores, which the compiler must take for stores to xs, too
 #pragma unroll
                 for (uint32_t j = 0; j < 16; ++j) xs[j] = J.xs[m0 + min(c + j, toks - 1)];
-                __syncwarp();  // rows past the end skip the stores below
-                tmem_ld16(lane_base + c, acc);
+                load_sums(c, acc);
                 if (r < J.rows) {
 #pragma unroll
                     for (uint32_t j = 0; j < 16; ++j)
@@ -309,7 +334,7 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
 #pragma unroll 1
             for (uint32_t c = 0; c < toks; c += 16) {
                 uint32_t acc[16];
-                tmem_ld16(lane_base + c, acc);
+                load_sums(c, acc);
 #pragma unroll
                 for (uint32_t j = 0; j < 16; j += 4) {
                     if (c + j >= toks) break;
@@ -350,8 +375,8 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
         }
     }
     if (J.n_out && warp < 4) {
-        epilogue_sync();  // this CTA's part of Y is written
-        add_outliers<DT>(J, n0, m0, toks, rank, parts, tid);
+        epilogue_sync<128>();  // this CTA's part of Y is written
+        add_outliers<DT>(J, n0, m0, toks, rank, parts, tid, 128);
     }
     tc_fence_before();
     __syncthreads();
@@ -374,8 +399,10 @@ __global__ void __launch_bounds__(kA8Threads, 2) eq_gemm_a8_split_kernel(const _
 //             accumulator's previous tile ("free"), then per slab waits for
 //             "full", issues 4 MMAs, commits to "empty" in both CTAs; at the
 //             end commits to "done" of the accumulator in both
-//   epilogue  (each CTA) 4 warps: waits for "done", reads its 128 rows x 256
-//             tokens, scales, stores, arrives on CTA 0's "free"
+//   epilogue  (each CTA) 8 warps, a thread one row and half of the tokens: waits
+//             for "done", takes the accumulator to registers (E4M3: adds it
+//             to the parts of K before), arrives on CTA 0's "free"; behind the
+//             last part scales and stores
 constexpr uint32_t kPairTok = 256;
 constexpr uint32_t kPairRows = 2 * kRowsTile;
 constexpr uint32_t kPair8Stage = kWTile + 128 * kSlab;  // per CTA: 128 rows + 128 tokens of a slab
@@ -410,12 +437,10 @@ __device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// The parts of a tile's K that go through an accumulator of their own (kMaxChain).
-static_assert((uint64_t)(kMaxE4m3Cols / kSlab) * ((kMaxE4m3Cols / kSlab + kMaxChain - 1) / kMaxChain) <= 0xFFFFFFFFull,
-              "slab numbers of the parts");
+// The parts of a tile's K that go through an accumulator of their own.
 template <int DT>
 __device__ __forceinline__ uint32_t segments(uint32_t slabs) {
-    return DT == EQ_INT8 ? 1u : (slabs + kMaxChain - 1) / kMaxChain;
+    return DT == EQ_INT8 ? 1u : (slabs + kChain - 1) / kChain;
 }
 
 // Where a tile starts its walk through K (it wraps around): see the split kernel's loader.
@@ -423,14 +448,18 @@ __device__ __forceinline__ uint32_t first_slab(uint32_t local, uint32_t t_tiles,
     return (local % t_tiles * 3 + local / t_tiles * 7) % slabs;
 }
 
-// The epilogue of a cluster's tiles: one of four warps, for its 32 accumulator lanes.  False when a wait ran out
-// here or elsewhere.  A warp that gives up still goes through its tiles, without waiting or storing: the four meet
-// at a barrier in every tile with super weights, however much later than the others one of them learns of it.
+// The epilogue of a cluster's tiles: one of eight warps, for the 32 accumulator lanes that it reaches (warp % 4) and
+// half of the tokens.  False when a wait ran out here or elsewhere.  A warp that gives up still goes through its
+// tiles, without waiting or storing: the eight meet at a barrier in every tile with super weights, however much
+// later than the others one of them learns of it.
+// The parts' sum stays in registers.  Through Y (four warps, loads and stores of a part's outputs) 2048 tokens x 8192 x
+// 28672 took 437 us in 3 parts and 680 in 14, here 417 to 435 in 14.
 template <int DT>
 __device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, uint32_t n_clusters, uint32_t rank,
                                               uint32_t tmem, uint32_t done0, uint32_t free_c0,
                                               const volatile uint32_t *abort, uint32_t warp, uint32_t lane) {
-    const uint32_t row = warp * 32u + lane;
+    constexpr uint32_t kTok = kPairTok / 2;
+    const uint32_t row = (warp & 3u) * 32u + lane, tok0 = (warp >> 2) * kTok;
     bool ok = true;
     uint32_t ti = 0;
     for (uint32_t tile = cl, jb = 0; tile < P.total_units; tile += n_clusters) {
@@ -443,6 +472,10 @@ __device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, ui
         const float ws = r < J.rows ? J.ws[r] : 0.f;
         if (J.n_out && local == 0 && warp == 0 && rank == 0) check_outliers(J, lane, 32, P.status);
         const uint32_t segs = segments<DT>((J.cols + kSlab - 1) / kSlab);
+        uint32_t sum[kTok];  // int32 or fp32 bits
+#pragma unroll
+        for (uint32_t j = 0; j < kTok; ++j) sum[j] = 0u;
+#pragma unroll 1
         for (uint32_t seg = 0; seg < segs && ok; ++seg, ++ti) {
             const uint32_t a = ti & 1u;
             if (!warp_wait(done0 + 8 * a, (ti >> 1) & 1u)) {
@@ -450,49 +483,44 @@ __device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, ui
                 break;
             }
             tc_fence_after();
-            const uint32_t acc0 = tmem + ((warp * 32u) << 16) + a * kPairTok;
-            const bool first = seg == 0, last = seg + 1 == segs;
-#pragma unroll 1
-            for (uint32_t c = 0; c < kPairTok && m0 + c < P.tokens; c += 32) {
-                uint32_t acc[32];
-                float xs[32];  // before the stores, which the compiler must take for stores to xs, too
+            const uint32_t acc0 = tmem + (((warp & 3u) * 32u) << 16) + a * kPairTok + tok0;
 #pragma unroll
-                for (uint32_t j = 0; j < 32; ++j) xs[j] = J.xs[min(m0 + c + j, P.tokens - 1)];
-                __syncwarp();  // the load is one instruction of the whole warp; rows past the end left the others' stores
-                tmem_ld32(acc0 + c, acc);
-                if (r >= J.rows) continue;
-                float *y = J.y + (size_t)(m0 + c) * J.rows + r;
-                if (first && last) {
+            for (uint32_t c = 0; c < kTok; c += 16) {
+                uint32_t acc[16];
+                tmem_ld16(acc0 + c, acc);
 #pragma unroll
-                    for (uint32_t j = 0; j < 32; ++j) {
-                        const uint32_t t = m0 + c + j;
-                        if (t < P.tokens) y[(size_t)j * J.rows] = scaled<DT>(acc[j], xs[j], ws);
-                    }
-                } else {  // Y holds the sum of the segments so far (this thread's own stores) until the last one
-#pragma unroll
-                    for (uint32_t j = 0; j < 32; ++j) {
-                        const uint32_t t = m0 + c + j;
-                        if (t >= P.tokens) continue;
-                        float v = __uint_as_float(acc[j]);
-                        if (!first) v = __fadd_rn(y[(size_t)j * J.rows], v);
-                        y[(size_t)j * J.rows] = last ? scaled<EQ_E4M3>(__float_as_uint(v), xs[j], ws) : v;
-                    }
-                }
+                for (uint32_t j = 0; j < 16; ++j)
+                    sum[c + j] = DT == EQ_INT8 ? acc[j]
+                                               : __float_as_uint(__fadd_rn(__uint_as_float(sum[c + j]), __uint_as_float(acc[j])));
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(free_c0 + 8 * a);
         }
+        if (ok) {
+            const uint32_t t0 = m0 + tok0;
+            float *y = J.y + (size_t)t0 * J.rows + r;
+#pragma unroll
+            for (uint32_t c = 0; c < kTok; c += 8) {
+                float xs[8];  // before the stores, which the compiler must take for stores to xs, too
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) xs[j] = J.xs[min(t0 + c + j, P.tokens - 1)];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j, y += J.rows)
+                    if (r < J.rows && t0 + c + j < P.tokens) *y = scaled<DT>(sum[c + j], xs[j], ws);
+            }
+        }
         if (J.n_out) {
-            epilogue_sync();  // the tile's Y is written
-            if (ok) add_outliers<DT>(J, r - row, m0, min(kPairTok, P.tokens - m0), 0, 1, row);
+            epilogue_sync<kPairEpilogue>();  // the tile's Y is written
+            if (ok)
+                add_outliers<DT>(J, r - row, m0, min(kPairTok, P.tokens - m0), 0, 1, warp * 32u + lane, kPairEpilogue);
         }
     }
     return ok;
 }
 
 template <int DT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     eq_gemm_a8_pair_kernel(const __grid_constant__ A8Params P) {
     constexpr uint32_t kStages = kPair8Stages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -517,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
         }
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(done0 + 8 * a, 1);
-            mbar_init(free0 + 8 * a, 8);  // (CTA 0) four epilogue warps of each CTA
+            mbar_init(free0 + 8 * a, 16);  // (CTA 0) eight epilogue warps of each CTA
         }
         fence_mbar_init();
         abort_s = 0;
@@ -531,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
     const uint32_t n_clusters = gridDim.x / 2, cl = blockIdx.x / 2;
     bool ok = true;
 
-    if (warp == 4) {
+    if (warp == 8) {
         // ---- loader (both CTAs) ----
         const uint32_t full_c0 = cluster_addr(full0, 0);
         uint32_t st = 0, ph = 0, g = 0;
@@ -565,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
         // that read them ("empty"; what is left of the last round)
         for (uint32_t k = g > kStages ? g - kStages : 0; k < g; ++k)
             if (!warp_wait(empty0 + 8 * (k % kStages), (k / kStages) & 1u)) ok = false;
-    } else if (warp == 5 && rank == 0) {
+    } else if (warp == 9 && rank == 0) {
         // ---- MMA (CTA 0) ----
         const uint64_t a0 = slab_desc(base), b0 = slab_desc(base + kWTile);
         uint32_t st = 0, ph = 0, ti = 0;  // ti: accumulators filled so far
@@ -579,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t n = slabs * (seg + 1) / segs - slabs * seg / segs;
+                const uint32_t n = slabs / segs + (seg < slabs % segs);
                 for (uint32_t k = 0; k < n; ++k) {
                     if (!warp_wait(full0 + 8 * st, ph)) {
                         ok = false;
@@ -606,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
         if (ok)
             for (uint32_t k = ti > 2 ? ti - 2 : 0; k < ti; ++k)
                 if (!warp_wait(done0 + 8 * (k & 1u), (k >> 1) & 1u)) ok = false;
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ---- epilogue (both CTAs) ----
         ok = pair_epilogue<DT>(P, cl, n_clusters, rank, tmem, done0, cluster_addr(free0, 0), &abort_s, warp, lane);
     }
@@ -623,11 +651,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kA8Threads, 1)
     }
 }
 
-// Failure-path check of the pair kernel's epilogue: its four warps on one tile of a job with super weights, whose
-// products are marked done.  Three of them store the tile and wait at its barrier; the last first runs out a bounded
+// Failure-path check of the pair kernel's epilogue: its eight warps on one tile of a job with super weights, whose
+// products are marked done.  Seven of them store the tile and wait at its barrier; the last first runs out a bounded
 // wait on a barrier that nothing arrives on, raises the abort flag, and enters as a warp that has given up.  The
 // block has to end, with EQ_DEV_TIMEOUT set and its tensor memory freed.
-__global__ void __launch_bounds__(128, 1) eq_a8_wait_timeout_kernel(const __grid_constant__ A8Params P) {
+__global__ void __launch_bounds__(kPairEpilogue, 1) eq_a8_wait_timeout_kernel(const __grid_constant__ A8Params P) {
     __shared__ __align__(8) uint64_t never_s, done_s[2], free_s[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile uint32_t abort_s;
@@ -642,7 +670,7 @@ __global__ void __launch_bounds__(128, 1) eq_a8_wait_timeout_kernel(const __grid
         mbar_init(never, 1);
         for (uint32_t a = 0; a < 2; ++a) {
             mbar_init(done0 + 8 * a, 1);
-            mbar_init(free0 + 8 * a, 8);
+            mbar_init(free0 + 8 * a, 16);
         }
         fence_mbar_init();
         abort_s = 0;
@@ -652,14 +680,14 @@ __global__ void __launch_bounds__(128, 1) eq_a8_wait_timeout_kernel(const __grid
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     const uint32_t zero[16] = {};
-    tmem_st16(tmem + ((warp * 32u) << 16), zero);
-    tmem_st16(tmem + ((warp * 32u) << 16) + 16, zero);
+    for (uint32_t c = 0; c < kPairTok / 2; c += 16)
+        tmem_st16(tmem + (((warp & 3u) * 32u) << 16) + (warp >> 2) * (kPairTok / 2) + c, zero);
     tmem_st_wait();
     tc_fence_before();
     __syncthreads();
     bool ok = true;
     if (warp == 0) warp_arrive(done0);
-    if (warp == 3 && !warp_wait(never, 0u)) {
+    if (warp == 7 && !warp_wait(never, 0u)) {
         ok = false;
         abort_s = 1;
         __syncwarp();
@@ -712,6 +740,10 @@ struct Shape {
     uint32_t parts;  // CTAs that share a tile's K
 };
 
+// Accumulators of `tok` tokens that fit a CTA's share of the tensor memory: half of it while two CTAs of the split
+// kernel fit an SM's shared memory (up to 64 tokens), so that neither waits for the other's.
+uint32_t max_accs(uint32_t tok) { return (tok <= 64 ? 256 : 512) / tok; }
+
 Shape pick_shape(const std::vector<const eq_a8_job *> &jobs, size_t at, size_t end, uint32_t tokens, uint32_t tok,
                  uint32_t sms, bool limited, bool chained) {
     if (limited) return {true, 1};
@@ -729,8 +761,10 @@ Shape pick_shape(const std::vector<const eq_a8_job *> &jobs, size_t at, size_t e
     const auto rounds = [](uint64_t n, uint64_t of) { return (n + of - 1) / of; };
     Shape best{true, 1};
     uint64_t best_cost = ~0ull;
-    // an E4M3 part's slabs go through one accumulator
-    const uint32_t least = chained ? (uint32_t)std::min<uint64_t>((slabs + kMaxChain - 1) / kMaxChain, kMaxSplit + 1) : 1;
+    // What an E4M3 part's accumulators reach.  Never more than 96 slabs: the estimate likes too few parts of a long K
+    // (64 tokens x 8192 x 28672: 44 us in three, 50 in the two that it would take).
+    const uint32_t reach = std::min(2 * kChain * max_accs(tok), 96u);
+    const uint32_t least = chained ? (uint32_t)std::min<uint64_t>((slabs + reach - 1) / reach, kMaxSplit + 1) : 1;
     for (uint32_t parts = least; parts <= kMaxSplit && (parts == 1 || 2ull * parts <= min_slabs); ++parts) {
         const uint64_t slab = std::max<uint64_t>(2 * tok, (kWTile + (uint64_t)tok * kSlab) / 40);
         const uint64_t sm = rounds(units * parts, sms) * rounds(slabs, parts) * slab;
@@ -777,18 +811,23 @@ int launch_type(const std::vector<const eq_a8_job *> &jobs, uint32_t tokens, uin
         if (!pair) {
             fn = (const void *)eq_gemm_a8_split_kernel<DT>;
             P.stage_bytes = kWTile + P.tok * kSlab;
-            P.tmem_cols = P.tok <= 32 ? 32 : P.tok <= 64 ? 64 : P.tok <= 128 ? 128 : 256;
             // two CTAs per SM up to 64 tokens: one's prologue and epilogue run under the other's loads
             const bool two = P.tok <= 64;
             smem = two ? kSplitSmem2 : kSplitSmem1;
             P.stages = std::min<uint32_t>(kMaxStages, (uint32_t)((smem - 1024) / P.stage_bytes));
             parts = shape.parts;
+            P.accs = 1;
+            if (DT == EQ_E4M3) {
+                const uint32_t most = ((jobs[at]->cols + kSlab - 1) / kSlab + parts - 1) / parts;  // slabs; longest K first
+                P.accs = std::min(max_accs(P.tok), (most + kChain - 1) / kChain);
+            }
+            for (P.tmem_cols = 32; P.tmem_cols < P.accs * P.tok;) P.tmem_cols *= 2;
             grid = (uint32_t)units * parts;
         }
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return EQ_ERR_CUDA;
         void *args[] = {&P};
-        if (!launch_overlapped(fn, grid, kA8Threads, smem, pair ? 0 : parts, args, s)) return EQ_ERR_CUDA;
+        if (!launch_overlapped(fn, grid, pair ? kPairThreads : kA8Threads, smem, pair ? 0 : parts, args, s)) return EQ_ERR_CUDA;
     }
     return EQ_OK;
 }
@@ -881,6 +920,6 @@ extern "C" EQW_API int eq_selftest_a8_wait_timeout(int32_t *d_status, cudaStream
     J.x8 = static_cast<const uint8_t *>(words);
     J.y = static_cast<float *>(words) + 7;
     J.rows = J.n_out = J.out_stride = 1, J.cols = 16;
-    eq_a8_wait_timeout_kernel<<<1, 128, 0, s>>>(P);
+    eq_a8_wait_timeout_kernel<<<1, kPairEpilogue, 0, s>>>(P);
     return cudaGetLastError() == cudaSuccess ? EQ_OK : EQ_ERR_CUDA;
 }

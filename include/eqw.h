@@ -462,9 +462,13 @@ EQW_API int eq_rmsnorm(const eq_rmsnorm_args *a, cudaStream_t s);
  *             + sum over super weights (r, c, v) of bf16(v) * x_scale[t] * x8[t, c]
  * x8 [tokens, cols] holds codes of the job's dtype (Int8 tokens with Int8
  * symbols, E4M3 with E4M3: what eq_rmsnorm writes), sym [rows, cols] what
- * eq_decode_symbols writes.  Int8: S is exact.  E4M3: exact products summed in
- * fp32 in a fixed order.  The results of one call do not depend on timing, but
- * the order of an E4M3 sum does depend on tokens, rows and cols.
+ * eq_decode_symbols writes.  Int8: S is exact.  E4M3: exact products, summed by
+ * the tensor cores over at most 32 slabs of 128 columns (their fp32 accumulator
+ * rounds towards zero), and those sums in fp32, rounded to nearest, in a fixed
+ * order: 1.2e-7 to 2.4e-7 of the result's norm at any cols, where fp32 products
+ * summed one after the other are 0.7e-7 to 2.8e-7 off.  The results of one call
+ * do not depend on timing, but the order of an E4M3 sum does depend on tokens,
+ * rows and cols.
  * Needs cols % 16 == 0, cols > 0, and cols <= 131056 for Int8, 2^26 for E4M3
  * (EQ_ERR_UNSUPPORTED otherwise); at most 2^31 - 256 rows and tokens.  sym and x8 16-byte aligned, contiguous rows.
  * Super weights: n_out entries sorted by row, as three arrays whose entries are
@@ -568,7 +572,7 @@ EQW_API int eq_build_checked(void);
 EQW_API int eq_selftest_gemm_wait_timeout(int32_t *d_status, cudaStream_t s);
 
 /*
- * The same check for the epilogue of eq_gemm_a8's pair kernel: one of its four
+ * The same check for the epilogue of eq_gemm_a8's pair kernel: one of its eight
  * warps gives up (on a barrier that nothing arrives on, after about a second)
  * while the others wait for it at a tile's barrier; the block still ends, with
  * EQ_DEV_TIMEOUT in *d_status and its TMEM freed.

@@ -30,11 +30,10 @@ def test_e4m3_columns(lib, cols, code):
     assert _call(lib, 0, cols=cols, dtype=INT8) == UNSUPPORTED
 
 
-def test_parts_of_k_within_32_bits():
-    """The kernel's split of the slabs into parts, in 32 bits and without a limit, at the widest accepted matrix."""
-    for cols in ((1 << 26), (1 << 26) - 16, 12288, 12304, 28672):
+def test_parts_of_k():
+    """The kernel's split of the slabs into chains, at the widest accepted matrix and around multiples of a chain."""
+    for cols in ((1 << 26), (1 << 26) - 16, 16, 2048, 2064, 12288, 12304, 28672):
         slabs = -(-cols // 128)
-        segs = -(-slabs // 96)
-        wide = [slabs * s // segs for s in range(segs + 1)]
-        assert wide == [((slabs * s) & 0xFFFFFFFF) // segs for s in range(segs + 1)]
-        assert all(0 < b - a <= 96 for a, b in zip(wide, wide[1:])) and wide[-1] == slabs
+        segs = -(-slabs // 16)
+        wide = [slabs // segs + (s < slabs % segs) for s in range(segs)]
+        assert all(0 < n <= 16 for n in wide) and sum(wide) == slabs
