@@ -48,9 +48,8 @@ constexpr uint32_t kA8Threads = 192;                     // split: 4 epilogue wa
 constexpr uint32_t kPairThreads = 320;                   // pairs: 8 epilogue warps, the loader warp, the MMA warp
 constexpr uint32_t kPairEpilogue = 256;                  // their threads
 constexpr uint32_t kMaxSplit = 8;
-constexpr uint32_t kMaxRows = 0x7FFFFF00u;               // tensor-map coordinates are 32-bit signed
+constexpr uint32_t kMaxRows = 0x7FFFFF00u;               // (and columns) tensor-map coordinates are 32-bit signed
 constexpr uint32_t kMaxInt8Cols = 131056;                // 128 * 128 * cols < 2^31
-constexpr uint32_t kMaxE4m3Cols = 1u << 26;              // far inside 32-bit slab numbers and coordinates
 // E4M3: the tensor core rounds its accumulator towards zero at every step, so a chain's error is a bias that grows
 // with its length. Relative to the result's norm, one accumulator for all of K: 2.3e-7 at 32 slabs, 5.0e-7 at 64, 2.5e-6
 // at 224; fp32 products summed in order by a library: 0.9e-7, 1.3e-7, 2.8e-7. So K is cut into chains with an
@@ -720,7 +719,7 @@ int check_job(const eq_a8_job &j, uint32_t tokens) {
     if (j.dtype != EQ_INT8 && j.dtype != EQ_E4M3) return EQ_ERR_INVALID_ARG;
     if (!j.rows) return EQ_OK;
     if (j.rows > kMaxRows) return EQ_ERR_UNSUPPORTED;
-    if (!j.cols || j.cols % 16 || j.cols > (j.dtype == EQ_INT8 ? kMaxInt8Cols : kMaxE4m3Cols)) return EQ_ERR_UNSUPPORTED;
+    if (!j.cols || j.cols % 16 || j.cols > (j.dtype == EQ_INT8 ? kMaxInt8Cols : kMaxRows)) return EQ_ERR_UNSUPPORTED;
     if (!j.sym || !j.scale || (tokens && (!j.x8 || !j.x_scale || !j.y))) return EQ_ERR_INVALID_ARG;
     const auto at = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
     if (at(j.sym) % 16 || at(j.x8) % 16 || at(j.scale) % 4 || at(j.x_scale) % 4 || at(j.y) % 4)

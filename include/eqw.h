@@ -469,8 +469,9 @@ EQW_API int eq_rmsnorm(const eq_rmsnorm_args *a, cudaStream_t s);
  * summed one after the other are 0.7e-7 to 2.8e-7 off.  The results of one call
  * do not depend on timing, but the order of an E4M3 sum does depend on tokens,
  * rows and cols.
- * Needs cols % 16 == 0, cols > 0, and cols <= 131056 for Int8, 2^26 for E4M3
- * (EQ_ERR_UNSUPPORTED otherwise); at most 2^31 - 256 rows and tokens.  sym and x8 16-byte aligned, contiguous rows.
+ * Needs cols % 16 == 0, cols > 0, and cols <= 131056 for Int8 (EQ_ERR_UNSUPPORTED
+ * otherwise); at most 2^31 - 256 rows, tokens and columns.  sym and x8 16-byte
+ * aligned, contiguous rows.
  * Super weights: n_out entries sorted by row, as three arrays whose entries are
  * out_stride elements apart (1: plain arrays, 3: the container's records); one
  * outside the matrix is skipped and reported (EQ_DEV_BAD_OUTLIER), entries out

@@ -21,19 +21,20 @@ def _call(lib, tokens, **kw):
     return lib.load().eq_gemm_a8((lib.eq_a8_job * 1)(lib.eq_a8_job(**a)), 1, tokens, FAKE, None)
 
 
-@pytest.mark.parametrize("cols,code", [(1 << 26, OK), ((1 << 26) + 16, UNSUPPORTED), (642000 * 128, UNSUPPORTED),
-                                       (1 << 31, UNSUPPORTED), ((1 << 32) - 16, UNSUPPORTED)])
+@pytest.mark.parametrize("cols,code", [(1 << 26, OK), (642000 * 128, OK), (0x7FFFFF00, OK),
+                                       (0x7FFFFF10, UNSUPPORTED), (1 << 31, UNSUPPORTED), ((1 << 32) - 16, UNSUPPORTED)])
 def test_e4m3_columns(lib, cols, code):
-    """Beyond 2^26 columns the numbers of slabs and parts of K pass 32 bits: the kernel would wait for slabs that
-    never come, or skip some."""
+    """Coordinates of the copies are signed 32-bit numbers: beyond 2^31 they would skip products."""
     assert _call(lib, 0, cols=cols) == code
     assert _call(lib, 0, cols=cols, dtype=INT8) == UNSUPPORTED
 
 
 def test_parts_of_k():
-    """The kernel's split of the slabs into chains, at the widest accepted matrix and around multiples of a chain."""
-    for cols in ((1 << 26), (1 << 26) - 16, 16, 2048, 2064, 12288, 12304, 28672):
-        slabs = -(-cols // 128)
-        segs = -(-slabs // 16)
-        wide = [slabs // segs + (s < slabs % segs) for s in range(segs)]
-        assert all(0 < n <= 16 for n in wide) and sum(wide) == slabs
+    """The kernel's split of the slabs into chains, at the widest accepted matrix and around multiples of a chain:
+    every product and sum below 2^32."""
+    for cols in (0x7FFFFF00, 642000 * 128, 16, 2048, 2064, 12288, 12304, 28672):
+        slabs = (cols + 127) // 128
+        segs = (slabs + 15) // 16
+        n, more = slabs // segs, slabs % segs
+        assert n + (more > 0) <= 16 and n > 0 and n * segs + more == slabs
+        assert cols + 127 < 2 ** 32 and slabs * 128 <= 2 ** 31

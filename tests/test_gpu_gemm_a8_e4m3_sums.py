@@ -45,3 +45,24 @@ def test_e4m3_sums_are_as_exact_at_any_width(eqw, tokens, rows, cols):
     depth = 128 + 32 + cols / 2048 + 8
     assert (err <= depth * 2.0 ** -22 * (x.abs() @ w.abs().t()) * sc + ref.abs() * 2.0 ** -22).all()
     assert float(err.norm() / ref.norm()) < 1.25 * 2.3e-7
+
+
+@pytest.mark.parametrize("cols", [(1 << 24) + 16, 90_000_000])
+def test_very_wide_matrices(eqw, cols):
+    """More chains than 32-bit products of slabs and chains could number.  Few nonzero whole numbers: exact."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows, tokens, n = 3, 2, 4096
+    at = torch.randint(0, cols, (n,), generator=g, device="cuda").unique()
+    at = torch.cat((at, torch.tensor([0, 1, cols - 17, cols - 1], device="cuda"))).unique()
+    w = torch.randint(1, 5, (rows, at.numel()), generator=g, device="cuda")
+    x = torch.randint(-4, 5, (tokens, at.numel()), generator=g, device="cuda")
+    sym, x8 = (torch.zeros(k, cols, dtype=torch.uint8, device="cuda") for k in (rows, tokens))
+    sym[:, at] = w.to(torch.int8).to(torch.float8_e4m3fn).view(torch.uint8)
+    x8[:, at] = x.to(torch.int8).to(torch.float8_e4m3fn).view(torch.uint8)
+    y = torch.empty(tokens, rows, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    eqw.gemm_a8(sym, torch.ones(rows, device="cuda"), x8.view(torch.float8_e4m3fn), torch.ones(tokens, device="cuda"),
+                y, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    assert torch.equal(y.double(), x.double() @ w.double().t())
