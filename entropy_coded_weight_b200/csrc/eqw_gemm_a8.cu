@@ -22,8 +22,8 @@
 // tokens are bound by memory, one Int8 token x 8192 x 8192 in 14.1 us (4.8 TB/s; about
 // 3 us are launch, first copies and the exchange of sums), 48 E4M3 tokens x 28672 x
 // 8192 in 40 us (5.9 TB/s).  Many are bound by the tensor cores and their power:
-// 4096 tokens x 28672 x 8192 in 626 us Int8 (3.07 POP/s, tensor pipe 93 % of active
-// clocks) and 770 to 800 us E4M3 (2.4 to 2.5 PFLOP/s at a lower clock).
+// 4096 tokens x 28672 x 8192 in 626 to 667 us Int8 (2.9 to 3.1 POP/s, tensor pipe 93 %
+// of active clocks) and 750 to 850 us E4M3 (2.3 to 2.6 PFLOP/s at a lower clock).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -451,7 +451,7 @@ __device__ __forceinline__ uint32_t first_slab(uint32_t local, uint32_t t_tiles,
 // half of the tokens.  False when a wait ran out here or elsewhere.  A warp that gives up still goes through its
 // tiles, without waiting or storing: the eight meet at a barrier in every tile with super weights, however much
 // later than the others one of them learns of it.
-// The parts' sum stays in registers.  Through Y (four warps, loads and stores of a part's outputs) 2048 tokens x 8192 x
+// The parts' sum stays in registers (128 of 168; a few loop values spill, 40 bytes).  Through Y (four warps, loads and stores of a part's outputs) 2048 tokens x 8192 x
 // 28672 took 437 us in 3 parts and 680 in 14, here 417 to 435 in 14.
 template <int DT>
 __device__ __forceinline__ bool pair_epilogue(const A8Params &P, uint32_t cl, uint32_t n_clusters, uint32_t rank,
@@ -733,7 +733,12 @@ int check_job(const eq_a8_job &j, uint32_t tokens) {
 // Launch shape.  Estimated SM clocks decide, from what one SM does: a split CTA's slab takes max(2 tok
 // (products), bytes / 40 (copies)), a pair's 512 (both); memory delivers about 23 bytes per clock and SM
 // when all run.  A round of CTAs costs about 4000 clocks besides (set-up, first copies, epilogue), sums
-// that meet over the cluster 2000 more.
+// that meet over the cluster 2000 more; the pairs' one round 8000 (a pair starts together, its last epilogue is
+// 256 x 256).  8192 x 8192, us split and pairs, the estimate's choice in brackets:
+//   tokens     32          65          128         256         512         1024
+//   Int8   [16.5] 24.5 [17.9] 24.7 [21.4] 26.1  31.4 [27.0] 41.1 [33.9] 77.7 [59.3]
+//   E4M3   [16.7] 25.1 [18.2] 25.5 [21.9] 27.1  32.9 [29.4] 46.0 [39.3] 85.0 [68.0]
+// 131 x 4104 x 11008 Int8 [18.7] 35.1; 300 x 28672 x 8192 Int8 138 [96]; 256 x 8192 x 28672 E4M3 86 [88].
 struct Shape {
     bool pair;
     uint32_t parts;  // CTAs that share a tile's K

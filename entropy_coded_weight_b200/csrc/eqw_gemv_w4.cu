@@ -33,11 +33,16 @@
 // shared memory in a fixed order; where there are fewer row tiles than SMs, the
 // CTAs of a cluster share K and their totals meet over distributed shared memory.
 //
-// Measured (B200): one token x 18944 x 8192, groups of 128: 19.7 us, 4.1 TB/s; 75776 x
-// 8192: 67 to 71 us for one token, 75 for eight, 84 for 16 (memory: 49).  The decoders
+// Measured (B200): one token x 18944 x 8192, groups of 128: 20 us, 4.0 TB/s; 75776 x
+// 8192: 67 to 75 us for one token, 75 for eight, 84 for 16 (memory: 49).  The decoders
 // bound it: issue slots, logic pipe and tensor pipe are 55, 58 and 13 % busy, the rest
 // are their waits.  The same product with mma.sync took 81 us for one token and 97
 // for eight.
+// Those rows fill the SMs evenly (one and four tiles of 128 each).  28672 x 8192 is 224
+// tiles, two rounds for 1.5 rounds' rows: eight tokens with zero points 37 to 39 us
+// (memory: 19), 32 tokens 67.  Groups of 32, whose sums leave tensor memory four times as
+// often: 49 us for one token, 60 for eight, 93 for 32 with a table.  4096 x 4096 takes
+// 6.3 us (memory: 1.3), most of it start and end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -76,7 +81,9 @@ struct W4Shape {
     static constexpr uint32_t kACols = kSlab / 2;            // tensor-memory columns of a decoded slab
     static constexpr int kGroups = (int)kSlab / (32 * GB);   // groups per slab
     // Stages and groups of decoders.  32 tokens: the totals take the registers, and with groups of 32 columns the
-    // accumulators the tensor memory.  Five and six stages of 128 columns measured like four.
+    // accumulators the tensor memory.  Five and six stages of 128 columns measured like four.  At four stages
+    // (80 registers) groups of 32 spill 24 to 32 bytes with 8 tokens and 8 with 16; with 32 tokens table codes
+    // spill 80 there, zero points 8 in groups of 64.
     static constexpr uint32_t kParts = kSlab == 256 ? 3 : TOK <= 16 ? 4 : GB > 1 ? 3 : 2;
     static constexpr uint32_t kThreads = kParts * 160 + 32;
     static constexpr uint32_t kRing = 12 * 128 / kSlab;      // slabs of codes
@@ -94,7 +101,7 @@ struct W4Shape {
 };
 
 struct W4Job {
-    CUtensorMap tmap_q;  // uint8 [rows, cols / 2], box 64 bytes x tile rows, 64-byte swizzle
+    CUtensorMap tmap_q;  // uint8 [rows, cols / 2], box kRowBytes x tile rows, swizzle of that width
     const void *scales;
     const uint8_t *zeros;
     const uint16_t *x;

@@ -19,12 +19,16 @@
 // root mean square.  Rows of ordinary size pay one comparison per thread and one per row.
 //
 // Bound by memory: x and res are read once, res_out, out and the scale written
-// once; a token's h stays in registers between the sum and the output.  One
+// once; a thread keeps its part of a token's h between the sum and the output.  One
 // row (token) is shared by T threads that hold E values each, as vectors of 8
 // consecutive columns (16-byte loads and stores) where the buffers allow it, else
-// column by column (coalesced, any width and address).
-// Measured (B200): 8192 tokens x 8192, fp32 x, bf16 residual, E4M3 out: 101 us,
-// 6.0 TB/s, 0.91 of a plain copy's rate; one token x 8192: 3.1 us, the launch.
+// column by column (coalesced, any width and address).  Up to 16 values (16384
+// columns) they stay in registers, column by column up to 8; with 32 values, and
+// with 16 column by column, 8 to 264 bytes per thread go through local memory.
+// Measured (B200): 8192 tokens x 8192, fp32 x, bf16 residual, E4M3 out: 102 us,
+// 5.9 TB/s, 0.9 of a plain copy's rate; one token x 8192: 3.1 us, the launch.  With a
+// block of 512 threads and more, few blocks fit an SM: 2000 x 16384, the same types, 61 us
+// (0.74), 2000 x 28672 in bf16 91 us (0.68).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -426,9 +430,10 @@ extern "C" EQW_API int eq_rmsnorm(const eq_rmsnorm_args *a, cudaStream_t s) {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return EQ_ERR_CUDA;
-    // values per thread: few while there are few rows per SM (a row's latency counts), else twice as many
+    // Values per thread: few while there are few rows per SM (a row's latency counts), else twice as many
     // (half the barriers' weight).  515 x 5121 bf16 + fp32: 10.2 us with 8, 12.2 with 16; 8192 x 8192 fp32 + bf16:
-    // 114 and 103; 1111 x 4096: 10.1 and 9.5.
+    // 114 and 103; 1111 x 4096: 10.1 and 9.5.  Rows only are counted, not how many blocks of their width fit: the
+    // first takes two rounds of blocks (two of 672 threads per SM), the last too (five of 256).
     uint32_t e = a->tokens <= 4 * (uint32_t)sms ? 8 : 16;
     const uint32_t span = a->cols + (mode == kShifted ? 7 : 0);
     while (e < kMaxPerThread && (uint64_t)e * kMaxThreads < span) e *= 2;

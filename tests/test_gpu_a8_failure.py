@@ -1,7 +1,7 @@
 """A wait that gives up in the 8-bit GEMM's pair kernel ends the kernel.
 
 eq_selftest_a8_wait_timeout runs the kernel's own epilogue on a tile with super
-weights: three warps reach the tile's barrier, the fourth gives up a wait on a
+weights: seven warps reach the tile's barrier, the eighth gives up a wait on a
 barrier that nothing arrives on and learns only then that the launch has failed.
 It has to reach the barrier all the same, or the block never ends.
 """
